@@ -246,6 +246,15 @@ __device__ __forceinline__ int item_units(const DecodeParams &p, int b) {
     return length_units<TILE>(p, p.seq_lens[b]);
 }
 
+// What becomes of a row's sum of weights: the factor of its O, and its LSE
+// from m in log2 units.  A sum is 0 where no key was visible (else it holds m's
+// own weight, 1 or more), which leaves O = 0 and LSE = -inf; NaN, from a NaN
+// among the row's query and keys, goes on to both.
+__device__ __forceinline__ float over_sum(float x, float sum) { return sum == 0.f ? 0.f : x / sum; }
+__device__ __forceinline__ float log_sum(float m, float sum) {
+    return sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
+}
+
 // O = 0, LSE = -inf for every row of sequence b, which has no keys.
 template <int D>
 __device__ void write_empty_sequence(const DecodeParams &p, int b) {
@@ -749,10 +758,9 @@ __global__ void __launch_bounds__(kDecodeThreads, (DecodeConfig<D, NT, RW, F8>::
                 if (whole) {
                     const int row = row0 + tid, head = p.Nq == 1 ? row : row / p.Nq, n = row - head * p.Nq;
                     const int hq = cur.h * p.group + head;
-                    scale = sum > 0.f ? dv / sum : 0.f;
+                    scale = over_sum(dv, sum);
                     sm_out[tid] = cur.b * p.os[0] + hq * p.os[1] + n * p.os[2];
-                    p.lse[(static_cast<int64_t>(cur.b) * p.Hq + hq) * p.Nq + n] =
-                        sum > 0.f ? (mx + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+                    p.lse[(static_cast<int64_t>(cur.b) * p.Hq + hq) * p.Nq + n] = log_sum(mx, sum);
                 } else {
                     p.part_ml[part0 + tid] = make_float2(mx, sum);
                 }
@@ -857,9 +865,6 @@ __global__ void __launch_bounds__(kMergeThreads, 4) fa_decode_merge_kernel(const
     const int head = p.Nq == 1 ? row : row / p.Nq, n = row - head * p.Nq, hq = h * p.group + head;
     __nv_bfloat16 *const out = p.o + b * p.os[0] + hq * p.os[1] + n * p.os[2];
     float *const lse = p.lse + (static_cast<int64_t>(b) * p.Hq + hq) * p.Nq + n;
-    const auto finish = [](float sum, float mx) {
-        return sum > 0.f ? (mx + log2f(sum)) * 0.6931471805599453f : -INFINITY;
-    };
     const auto place = [&](int x) { return static_cast<int64_t>(x == 0 ? job.slot : 2 * (cta + x)) * p.part_rows + r; };
     const int step = alone ? 1 : kMergeWarps;
     Vec v[kMergeBatch];
@@ -894,13 +899,13 @@ __global__ void __launch_bounds__(kMergeThreads, 4) fa_decode_merge_kernel(const
             const float wy = __shfl_sync(0xffffffffu, w, y);
             if (y < parts) add(o, wy, y);
         }
-        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        const float inv = over_sum(1.f, sum);
         uint32_t packed[PER / 2];
         #pragma unroll
         for (int c = 0; c < PER / 2; ++c) packed[c] = ptx::pack_bf16x2(o[2 * c] * inv, o[2 * c + 1] * inv);
         if constexpr (PER == 4) reinterpret_cast<uint2 *>(out)[lane] = make_uint2(packed[0], packed[1]);
         else reinterpret_cast<uint32_t *>(out)[lane] = packed[0];
-        if (lane == 0) *lse = finish(sum, mx);
+        if (lane == 0) *lse = log_sum(mx, sum);
         return;
     }
 
@@ -951,7 +956,7 @@ __global__ void __launch_bounds__(kMergeThreads, 4) fa_decode_merge_kernel(const
     for (int c = 0; c < PER; ++c) sm_o[warp][lane * PER + c] = o[c];
     __syncthreads();
     if (tid < D / 2) {
-        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        const float inv = over_sum(1.f, sum);
         float y0 = 0.f, y1 = 0.f;
         #pragma unroll
         for (int w = 0; w < kMergeWarps; ++w) {
@@ -961,7 +966,7 @@ __global__ void __launch_bounds__(kMergeThreads, 4) fa_decode_merge_kernel(const
         }
         reinterpret_cast<uint32_t *>(out)[tid] = ptx::pack_bf16x2(y0 * inv, y1 * inv);
     }
-    if (tid == 0) *lse = finish(sum, mx);
+    if (tid == 0) *lse = log_sum(mx, sum);
 }
 
 }  // namespace fa

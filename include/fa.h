@@ -516,8 +516,10 @@ fa_status fa_paged_append(const void *Q, const int64_t *q_strides, void *Qr, con
  *            afterwards.  Calls that share it must not overlap in time
  * O, LSE and the workspace overlap neither each other nor the inputs.
  * Cache rows at and past a sequence's length are not read: they may hold
- * anything.  The result does not depend on what else is in the batch beyond
- * the order in which slices are joined; the same call gives the same bits.
+ * anything.  A NaN among a row's query and the keys that it sees makes its O
+ * and LSE NaN, so that LSE = -inf keeps its meaning.  The result does not
+ * depend on what else is in the batch beyond the order in which slices are
+ * joined; the same call gives the same bits.
  * Errors: as fa_fwd_paged; FA_ERR_UNSUPPORTED also for Nq > 16;
  * FA_ERR_INVALID_ARG for Hq % Hkv, cache_type, a NULL descale with
  * FA_CACHE_E4M3, |scale| log2(e) past fp32's range, a bad stride, a NULL or too
