@@ -6,12 +6,13 @@
 // and the gradient turns by -phi.
 //
 // The phase.  cos and sin need phi only modulo a turn.  f_c / (2 pi) is held
-// as a 64-bit fraction of a turn, F_c = f_c / (2 pi) * 2^64 mod 2^64; then
-// pos * F_c mod 2^64, one wrapping integer product, is the phase of any
-// int32 position to within |pos| 2^-65 turns, with no range reduction in
-// floating point (an fp32 angle is off by 0.06 rad at position 10^6).  The
-// nearest quarter turn is its top bits, and what is left, at most an eighth
-// of a turn, goes through the Taylor polynomials of sin and cos.
+// as a 64-bit fraction of a turn, F_c = f_c / (2 pi) * 2^64 mod 2^64, rounded
+// once (rotary_phase.h); then pos * F_c mod 2^64, one wrapping integer product,
+// is the phase of any int32 position to within |pos| 2^-65 turns, with no range
+// reduction in floating point (an fp32 angle is off by 0.06 rad at position
+// 10^6).  Its upper 32 bits go on, cut off: up to 2^-32 turns (1.5e-9 rad) more.
+// The nearest quarter turn is their top bits, and what is left, at most an
+// eighth of a turn, goes through the Taylor polynomials of sin and cos.
 #pragma once
 
 #include <cstdint>

@@ -12,6 +12,7 @@
 #include "fa_block_tables_kernel.cuh"
 #include "fa_decode_kernel.cuh"
 #include "fa_rope_kernel.cuh"
+#include "rotary_phase.h"
 
 namespace {
 
@@ -146,18 +147,6 @@ fa_status take_strides(int64_t *out, const int64_t *given, const int *extent, in
     return FA_OK;
 }
 
-// f / (2 pi) turns as a 64-bit fraction of a turn: the product in two doubles
-// (the second holds what the first rounds away), each taken modulo 1.
-uint64_t phase_of(double f) {
-    constexpr double kHi = 0x1.45f306dc9c883p-3, kLo = -0x1.6b01ec5417056p-57;   // 1 / (2 pi)
-    const double hi = f * kHi;
-    const double lo = std::fma(f, kHi, -hi) + f * kLo;
-    const auto fraction = [](double x) {   // x - nearbyint(x) is exact, in [-1/2, 1/2]
-        return static_cast<uint64_t>(std::llrint(std::ldexp(x - std::nearbyint(x), 63))) * 2;
-    };
-    return fraction(hi) + fraction(lo);
-}
-
 // The rotation kernel for p: a CTA for each tile of tokens and group of heads,
 // in as small groups as still run at once, up to 8 heads.  More CTAs than fit
 // the GPU leave a second round half empty, fewer leave SMs idle: 3 x 1021
@@ -204,7 +193,7 @@ fa_status take_rotary(fa::RotaryTable &tab, int d, int rot, int axes, const doub
         std::memset(&made.tab, 0, sizeof made.tab);
         for (int c = 0; c < pairs; ++c) {
             if (!std::isfinite(inv_freq[c]) || axis[c] < 0 || axis[c] >= axes) return FA_ERR_INVALID_ARG;
-            made.tab.phase[c] = phase_of(inv_freq[c]);
+            made.tab.phase[c] = fa::rotary_phase(inv_freq[c]);
             made.tab.axis[c] = static_cast<uint8_t>(axis[c]);
         }
         std::memcpy(made.freq, inv_freq, pairs * sizeof(double));
