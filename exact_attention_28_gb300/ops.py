@@ -10,6 +10,8 @@ import ctypes
 import math
 import os
 import struct
+import threading
+import weakref
 
 import torch
 
@@ -497,21 +499,72 @@ def fa_rope(q, k, positions, rotary, q_out=None, k_out=None, inverse=False, stre
     return q_out, k_out
 
 
-def _mark_leaves(next_functions, dev):
-    """(the gradient nodes of leaves among a function's inputs, whether one of them belongs to another stream).
+class _Trail:
+    """Where the graph of one rotation begins: its device, its stream, and the edges to what its inputs came from."""
+    __slots__ = ("dev", "stream", "edges", "mixed", "__weakref__")
 
-    A leaf's node keeps the stream of the graph that made it for as long as
-    any graph of the leaf lives.  A captured backward that reaches a node of
-    another stream makes that stream wait inside the capture, which ends the
-    process; so graphs leave their stream on the node, and a captured backward
-    that finds another one there refuses."""
-    nodes, clash = [], False
-    for node, _ in next_functions:
+
+# The trails of the rotations whose graphs are alive: {device: {stream: WeakSet}}.
+#
+# The gradient node of a leaf keeps the stream of the graph that made it for as
+# long as any graph of the leaf lives.  A captured backward that reaches a node
+# of another stream makes that stream wait inside the capture, which ends the
+# process.  A node does not tell its stream, so a captured backward looks for
+# the living rotations of other streams that come from the same leaves, through
+# views, projections and whatever else lies between, and refuses.  That search
+# walks whole graphs, so it is left to captures: an eager call leaves its trail,
+# and its stream on the node of an input that is a leaf itself (where a graph of
+# another function may keep it longer than this one lives).
+_trails, _trails_lock = {}, threading.Lock()
+
+
+def _leaves_behind(edges):
+    """The gradient nodes of all leaves that a function's inputs came from."""
+    seen, leaves, todo = set(), set(), [node for node, _ in edges if node is not None]
+    while todo:
+        node = todo.pop()
+        if node in seen:
+            continue
+        seen.add(node)
         if type(node).__name__ == "AccumulateGrad":
-            stream = _raw_stream(dev)
-            clash = clash or node.metadata.setdefault("fa_stream", stream) != stream
-            nodes.append(node)      # the mark lives as long as the graph
-    return nodes, clash
+            leaves.add(node)
+        else:
+            todo.extend(n for n, _ in node.next_functions if n is not None)
+    return leaves
+
+
+def _living(trail, apart):
+    """The other living trails on this device whose leaves' nodes may belong to another stream than `apart`."""
+    with _trails_lock:
+        return [t for stream, live in _trails.get(trail.dev, {}).items() for t in live
+                if t is not trail and (stream != apart or t.mixed)]
+
+
+def _leave_trail(edges, dev):
+    """The trail of a rotation on the current stream.  `mixed`: nodes of its leaves may be another stream's all the
+    same, made by a rotation that was alive then."""
+    trail = _Trail()
+    stream = _raw_stream(dev)
+    trail.dev, trail.stream, trail.edges = dev, stream, edges
+    for node, _ in edges:
+        if type(node).__name__ == "AccumulateGrad":
+            node.metadata.setdefault("fa_stream", stream)
+    with _trails_lock:
+        streams = _trails.setdefault(dev, {})
+        if stream not in streams:
+            streams[stream] = weakref.WeakSet()
+        trail.mixed = len(streams) > 1 and any(live for s, live in streams.items() if s != stream)
+        streams[stream].add(trail)
+    if trail.mixed and torch.cuda.is_current_stream_capturing():
+        trail.mixed = _meets(trail)
+    return trail
+
+
+def _meets(trail):
+    """Whether a leaf behind this trail may have a node of another stream than the trail's."""
+    leaves = _leaves_behind(trail.edges)
+    return (any(node.metadata.get("fa_stream", trail.stream) != trail.stream for node in leaves) or
+            any(not leaves.isdisjoint(_leaves_behind(t.edges)) for t in _living(trail, trail.stream)))
 
 
 class _Rotation(torch.autograd.Function):
@@ -521,15 +574,17 @@ class _Rotation(torch.autograd.Function):
     def forward(ctx, q, k, positions, rotary, inverse):
         ctx.save_for_backward(positions)
         ctx.rotary, ctx.inverse = rotary, inverse
-        ctx.leaves, ctx.clash = _mark_leaves(ctx.next_functions, positions.get_device())
         q_out, k_out = fa_rope(_rows(q), None if k is None else _rows(k), positions, rotary, inverse=inverse)
+        edges = ctx.next_functions
+        if edges:
+            ctx.trail = _leave_trail(edges, positions.get_device())
         return q_out if k is None else (q_out, k_out)
 
     @staticmethod
     def backward(ctx, gq, gk=None):
         positions, = ctx.saved_tensors
-        if ctx.clash and torch.cuda.is_current_stream_capturing():
-            raise RuntimeError("apply_rotary: this backward is being captured while an eager graph of the same leaf, "
+        if torch.cuda.is_current_stream_capturing() and _meets(ctx.trail):
+            raise RuntimeError("apply_rotary: this backward is being captured while a graph of the same leaf, "
                                "made on another stream, is alive; drop that graph (its outputs) first")
         if torch.is_grad_enabled():     # a graph of the backward itself is asked for
             out = _Rotation.apply(gq, gk, positions, ctx.rotary, not ctx.inverse)
@@ -558,8 +613,10 @@ def apply_rotary(q, k, positions, rotary):
 
     Capturing its backward into a CUDA graph takes what PyTorch asks of any
     captured backward: warm up on the capture's stream, and let no eager graph
-    of the same leaves live on another one.  A captured backward that meets
-    one made by this function raises RuntimeError."""
+    of the same leaves live on another one.  A captured backward of a rotation
+    raises RuntimeError where a living rotation of another stream comes from a
+    leaf that its q or k comes from too, be q and k that leaf, views of it or
+    results of it.  Graphs that went through no rotation are not seen."""
     return _Rotation.apply(q, k, positions, rotary, False)
 
 
