@@ -128,9 +128,29 @@ fa_status serving_device(int &sms) {
     return FA_OK;
 }
 
+// Memory that a call reads or writes; at nullptr, or with no bytes: none, or
+// not told apart here (a strided tensor's rows may lie between other ones').
+struct Span {
+    const void *at;
+    int64_t bytes;
+    bool output;
+};
+// Whether no output lies on another span.
+template <int N>
+bool apart(const Span (&spans)[N]) {
+    for (const Span &x : spans)
+        for (const Span &y : spans) {
+            const char *a = static_cast<const char *>(x.at), *b = static_cast<const char *>(y.at);
+            if (&x != &y && x.output && a && b && x.bytes > 0 && y.bytes > 0 && a < b + y.bytes && b < a + x.bytes)
+                return false;
+        }
+    return true;
+}
+
 // Strides of a tensor [extent_0, .., extent_{n-1}, d] (contiguous when given
 // is NULL), checked: >= 0, rows on 16-byte boundaries, at most 2^40 elements;
-// an output's rows must not lie on one another.
+// an output's rows must not lie on one another: each stride reaches past all
+// that the smaller ones span.
 fa_status take_strides(int64_t *out, const int64_t *given, const int *extent, int n, int d, bool output) {
     int64_t s = d;
     bool absent = false;   // no heads: the tensor is not there
@@ -144,7 +164,41 @@ fa_status take_strides(int64_t *out, const int64_t *given, const int *extent, in
         if (output && extent[i] > 1 && out[i] < d) return FA_ERR_INVALID_ARG;
         if (extent[i] > 1 && out[i] % 8 != 0) return FA_ERR_MISALIGNED;
     }
+    if (output && !absent) {
+        __int128 span = d;
+        bool taken[3] = {};
+        for (int k = 0; k < n; ++k) {
+            int least = -1;
+            for (int i = 0; i < n; ++i)
+                if (!taken[i] && extent[i] > 1 && (least < 0 || out[i] < out[least])) least = i;
+            if (least < 0) break;
+            if (out[least] < span) return FA_ERR_INVALID_ARG;
+            span += static_cast<__int128>(out[least]) * (extent[least] - 1);
+            taken[least] = true;
+        }
+    }
     return FA_OK;
+}
+
+// An output that begins where its input does is the input itself: the same
+// strides.  `in` then counts as no other memory.
+bool in_place_ok(const void *&in, const int64_t *in_strides, const void *out, const int64_t *out_strides,
+                 const int *extent, int n) {
+    if (!in || in != out) return true;
+    for (int i = 0; i < n; ++i)
+        if (extent[i] > 1 && in_strides[i] != out_strides[i]) return false;
+    in = nullptr;
+    return true;
+}
+
+// Bytes of a bf16 tensor [extent_0, .., extent_{n-1}, d] where it is contiguous, else 0.
+int64_t whole_bytes(const int64_t *strides, const int *extent, int n, int d) {
+    int64_t s = d;
+    for (int i = n - 1; i >= 0; --i) {
+        if (extent[i] > 1 && strides[i] != s) return 0;
+        s *= extent[i];
+    }
+    return 2 * s;
 }
 
 // The rotation kernel for p: a CTA for each tile of tokens and group of heads,
@@ -225,18 +279,11 @@ extern "C" fa_status fa_block_tables(int *block_table, const int *ctx_lens, cons
                           static_cast<const void *>(counts)})
         if (!aligned(x, 4)) return FA_ERR_MISALIGNED;
     // CTAs read the lengths and the free list while others write: no output may lie on another array
-    const struct {
-        const int *at;
-        int64_t n;
-        bool output;
-    } arrays[] = {{ctx_lens, B, false}, {new_lens, B, false}, {free_blocks, num_free, false},
-                  {block_table, static_cast<int64_t>(B) * max_blocks, true}, {seq_lens, B, true},
-                  {query_start, int64_t{B} + 1, true}, {slots, num_tokens, true}, {positions, num_tokens, true},
-                  {counts, 2, true}};
-    for (const auto &x : arrays)
-        for (const auto &y : arrays)
-            if (&x != &y && x.output && x.n > 0 && y.n > 0 && x.at < y.at + y.n && y.at < x.at + x.n)
-                return FA_ERR_INVALID_ARG;
+    if (!apart<9>({{ctx_lens, int64_t{4} * B, false}, {new_lens, int64_t{4} * B, false},
+                   {free_blocks, int64_t{4} * num_free, false}, {block_table, int64_t{4} * B * max_blocks, true},
+                   {seq_lens, int64_t{4} * B, true}, {query_start, int64_t{4} * B + 4, true},
+                   {slots, int64_t{4} * num_tokens, true}, {positions, int64_t{4} * num_tokens, true}, {counts, 8, true}}))
+        return FA_ERR_INVALID_ARG;
     fa::BlockTableParams p;
     p.table = block_table;
     p.ctx = ctx_lens;
@@ -289,6 +336,11 @@ extern "C" fa_status fa_rope(const void *Q, const int64_t *q_strides, void *Qr, 
         if (s != FA_OK) return s;
     if (!aligned(Q, 16) || !aligned(Qr, 16) || !aligned(K, 16) || !aligned(Kr, 16) || !aligned(positions, 4))
         return FA_ERR_MISALIGNED;
+    const void *q_in = Q, *k_in = K;
+    if (!in_place_ok(q_in, p.qs, Qr, p.qos, qe, 3) || !in_place_ok(k_in, p.ks, Kr, p.kos, ke, 3) || Qr == Kr ||
+        !apart<4>({{q_in, whole_bytes(p.qs, qe, 3, d), false}, {k_in, whole_bytes(p.ks, ke, 3, d), false},
+                   {Qr, whole_bytes(p.qos, qe, 3, d), true}, {Kr, whole_bytes(p.kos, ke, 3, d), true}}))
+        return FA_ERR_INVALID_ARG;
     p.q = static_cast<const __nv_bfloat16 *>(Q);
     p.k = static_cast<const __nv_bfloat16 *>(K);
     p.qo = static_cast<__nv_bfloat16 *>(Qr);
@@ -342,6 +394,13 @@ extern "C" fa_status fa_paged_append(const void *Q, const int64_t *q_strides, vo
         !aligned(V_cache, 16) || !aligned(slots, 4) || !aligned(positions, 4) || !aligned(k_descale, 4) ||
         !aligned(v_descale, 4))
         return FA_ERR_MISALIGNED;
+    const void *q_in = Q;
+    const int64_t cache = rows * Hkv * d * (cache_type == FA_CACHE_E4M3 ? 1 : 2);
+    if (!in_place_ok(q_in, strides[0], Qr, strides[1], qe, 2) ||
+        !apart<7>({{q_in, whole_bytes(strides[0], qe, 2, d), false}, {K, whole_bytes(strides[2], ke, 2, d), false},
+                   {V, whole_bytes(strides[3], ke, 2, d), false}, {slots, int64_t{4} * T, false},
+                   {Qr, whole_bytes(strides[1], qe, 2, d), true}, {K_cache, cache, true}, {V_cache, cache, true}}))
+        return FA_ERR_INVALID_ARG;
     const auto run = [&](auto p) {
         p.q = static_cast<const __nv_bfloat16 *>(Q);
         p.k = static_cast<const __nv_bfloat16 *>(K);
@@ -444,6 +503,15 @@ extern "C" fa_status fa_decode_paged(const void *Q, const int64_t *q_strides, co
         !aligned(workspace, 256))
         return FA_ERR_MISALIGNED;
     const bool f8 = cache_type == FA_CACHE_E4M3;
+    const int64_t cache = static_cast<int64_t>(num_blocks) * Hkv * block_size * d * (f8 ? 1 : 2);
+    // O may be Q: only an item's own CTAs read its queries, and its O is written when they are done
+    const void *q_in = Q;
+    if (!in_place_ok(q_in, p.qs, O, p.os, e, 3) ||
+        !apart<8>({{q_in, whole_bytes(p.qs, e, 3, d), false}, {K_cache, cache, false}, {V_cache, cache, false},
+                   {block_table, int64_t{4} * B * max_blocks, false}, {seq_lens, int64_t{4} * B, false},
+                   {O, whole_bytes(p.os, e, 3, d), true}, {LSE, int64_t{4} * B * Hq * Nq, true},
+                   {workspace, static_cast<int64_t>(space.bytes), true}}))
+        return FA_ERR_INVALID_ARG;
     const DecodeLayout layout = decode_layout(p.rows);
     const int cap = decode_rows(layout);
     p.row_blocks = (p.rows + cap - 1) / cap;

@@ -381,8 +381,12 @@ fa_status fa_schedule(int B, int H, int Nq, int Nk, int d, int causal, int num_s
  * Stride arguments are host arrays of element counts, read before the call
  * returns; NULL means contiguous in the stated order.  The last dimension (d)
  * is always contiguous.  Strides are >= 0 and multiples of 8 (rows start on
- * 16-byte boundaries); those of an output are >= d wherever its extent is
- * more than 1.
+ * 16-byte boundaries); rows of an output do not lie on one another: of its
+ * dimensions with an extent above 1, each stride is at least d plus what the
+ * dimensions of smaller strides reach, sum (extent - 1) * stride.
+ * FA_ERR_INVALID_ARG also for an output on another argument's memory, wherever
+ * both are contiguous or begin at the same place (but for the in-place forms
+ * that are allowed); between strided tensors that is the caller's to see to.
  */
 
 /* Element type of a paged cache. */
@@ -514,7 +518,8 @@ fa_status fa_paged_append(const void *Q, const int64_t *q_strides, void *Qr, con
  *   workspace  device memory, 256-byte aligned, at least the bytes that
  *            fa_decode_paged_workspace returns; contents ignored and undefined
  *            afterwards.  Calls that share it must not overlap in time
- * O, LSE and the workspace overlap neither each other nor the inputs.
+ * O, LSE and the workspace overlap neither each other nor the inputs, but O may
+ * be Q itself with the same strides.
  * Cache rows at and past a sequence's length are not read: they may hold
  * anything.  A NaN among a row's query and the keys that it sees makes its O
  * and LSE NaN, so that LSE = -inf keeps its meaning.  The result does not

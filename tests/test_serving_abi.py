@@ -122,6 +122,54 @@ def test_decode_refusals(lib, kw, expected):
                                a["bs"], a["d"], a["scale"], a["causal"], a["ws"] or None, a["nbytes"], None) == expected
 
 
+ROPE_ARGS = ("q", "qs", "qo", "qos", "Hq", "k", "ks", "ko", "kos", "Hk", "pos", "pa", "pb", "B", "N", "d", "rot", "axes",
+             "freq", "axis", "inter", "inv")
+APPEND_ARGS = ("q", "qs", "qo", "qos", "Hq", "k", "ks", "v", "vs", "Hkv", "kc", "vc", "kind", "kd", "vd", "slots", "pos",
+               "pa", "T", "blocks", "bs", "d", "rot", "axes", "freq", "axis", "inter")
+DECODE_ARGS = ("q", "qs", "kc", "vc", "kind", "kd", "vd", "table", "seq", "o", "os", "lse", "B", "Hq", "Hkv", "Nq",
+               "max_blocks", "blocks", "bs", "d", "scale", "causal", "ws", "nbytes")
+
+
+def no_gpu():
+    return not torch.cuda.is_available()
+
+
+# Outputs on other memory, and layouts beside them that are allowed: without a GPU those get as far as CUDA's error.
+@pytest.mark.parametrize("fn,base,names,kw,refused", [
+    ("fa_rope", ROPE, ROPE_ARGS, kw, refused) for kw, refused in [
+        (dict(qos=strides(64, 64, 64)), True),                          # every head's rows on every other's
+        (dict(qos=strides(2048, 64, 64)), True), (dict(qos=strides(2048, 448, 64)), True),
+        (dict(qos=strides(0, 64, 192)), True),                          # 4 heads of 64 in rows of 192
+        (dict(qos=strides(0, 64, 256)), False), (dict(qos=strides(64, 512, 64)), False),      # token-major; one batch
+        (dict(B=2, qos=strides(1024, 512, 64)), True), (dict(B=2, qos=strides(64, 512, 128)), True),
+        (dict(B=2, qos=strides(64, 1024, 128)), False),                 # batches side by side
+        (dict(kos=strides(0, 64, 64)), True), (dict(Hk=1, kos=strides(0, 64, 64)), False),
+        (dict(qo=0x40000), True),                                       # q's output is k's
+        (dict(qo=0x10000), False), (dict(qo=0x10000, qos=strides(0, 64, 256)), True),         # in place, strides differ
+        (dict(qo=0x10080), True), (dict(qo=0x30000), True), (dict(ko=0x10000), True), (dict(qo=0x3f800), True),
+        (dict(ko=0x30000), False), (dict(qo=0x30000, qos=strides(0, 1024, 64)), False),       # strided: not told apart
+    ]] + [("fa_paged_append", APPEND, APPEND_ARGS, kw, refused) for kw, refused in [
+        (dict(qos=strides(64, 64)), True), (dict(qos=strides(256, 64)), False), (dict(qos=strides(64, 512)), False),
+        (dict(qos=strides(64, 448)), True), (dict(vc=0x50000), True), (dict(vc=0x51000), True), (dict(vc=0x52000), False),
+        (dict(vc=0x52000, kind=0), True), (dict(qo=0x10000), False), (dict(qo=0x10000, qos=strides(64, 512)), True),
+        (dict(qo=0x30000), True), (dict(qo=0x50100), True), (dict(kc=0x8fff0), True), (dict(vc=0x40000), True),
+    ]] + [("fa_decode_paged", DECODE, DECODE_ARGS, kw, refused) for kw, refused in [
+        (dict(Nq=2, os=strides(512, 128, 64)), False), (dict(Nq=2, os=strides(512, 64, 64)), True),
+        (dict(Nq=2, os=strides(64, 128, 512)), False), (dict(os=strides(64, 64, 64)), True),
+        (dict(o=0x10000), False), (dict(o=0x10000, os=strides(256, 128, 64)), True),            # in place, strides differ
+        (dict(o=0x10100), True), (dict(lse=0x80010), True), (dict(lse=0x70004), True), (dict(o=0x21000), True),
+        (dict(ws=0x8ff00), True), (dict(lse=0x100100), True), (dict(vc=0x20000), False),      # one cache for both: read only
+        (dict(o=0xfff00), True), (dict(seq=0x60000), False), (dict(ws=0x80200), True),
+    ]])
+def test_outputs_on_other_memory_are_refused(lib, fn, base, names, kw, refused):
+    if not refused and not no_gpu():
+        pytest.skip("the pointers are fakes")
+    a = dict(base, **kw)
+    pointers = {"q", "qo", "k", "ko", "v", "kc", "vc", "kd", "vd", "slots", "pos", "table", "seq", "o", "lse", "ws"}
+    status = getattr(lib, fn)(*[(a[n] or None) if n in pointers else a[n] for n in names], None)
+    assert status == (INV if refused else ops.FA_ERR_CUDA)
+
+
 def test_decode_workspace_needs_no_gpu_and_checks_its_sizes(lib):
     assert ops.decode_paged_workspace(1, 32, 8, 1, 128) > 0
     for bad in ((0, 1, 1, 1, 64), (1, 3, 2, 1, 64), (1, 1, 1, 17, 64), (1, 1, 1, 1, 80)):
