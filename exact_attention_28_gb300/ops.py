@@ -421,7 +421,7 @@ def fa_block_tables(block_table, ctx_lens, new_lens, free_blocks, block_size, nu
     """Block table, slots and positions of a step from the requests' lengths.
 
     block_table int32 [B, max_blocks] is updated in place; ctx_lens, new_lens
-    int32 [B]; free_blocks int32 [num_free] (all contiguous CUDA tensors).
+    int32 [B]; free_blocks int32 [num_free], or None (all contiguous CUDA tensors).
     num_tokens is the room for new tokens; those behind the last one get slot
     -1 and position 0.  Returns (seq_lens [B], query_start [B+1], slots
     [num_tokens], positions [num_tokens], counts [2]: tokens, blocks needed)."""
@@ -429,7 +429,7 @@ def fa_block_tables(block_table, ctx_lens, new_lens, free_blocks, block_size, nu
     if block_table.dim() != 2:
         raise ValueError("block_table must be [B, max_blocks]")
     B, max_blocks = block_table.shape
-    num_free = free_blocks.numel()
+    num_free = 0 if free_blocks is None else free_blocks.numel()
     if seq_lens is None:
         seq_lens = _new(B, _I32, dev, stream)
     if query_start is None:
@@ -442,7 +442,7 @@ def fa_block_tables(block_table, ctx_lens, new_lens, free_blocks, block_size, nu
         counts = _new(2, _I32, dev, stream)
     _call(dev, stream, (_lib or load_library()).fa_block_tables, _whole("block_table", block_table, _I32, dev),
           _flat("ctx_lens", ctx_lens, _I32, dev, B), _flat("new_lens", new_lens, _I32, dev, B),
-          _flat("free_blocks", free_blocks, _I32, dev, num_free), _flat("seq_lens", seq_lens, _I32, dev, B),
+          None if free_blocks is None else _flat("free_blocks", free_blocks, _I32, dev, num_free), _flat("seq_lens", seq_lens, _I32, dev, B),
           _flat("query_start", query_start, _I32, dev, B + 1), _flat("slots", slots, _I32, dev, num_tokens),
           _flat("positions", positions, _I32, dev, num_tokens), _flat("counts", counts, _I32, dev, 2),
           B, max_blocks, block_size, num_free, num_tokens)
@@ -474,7 +474,8 @@ def fa_rope(q, k, positions, rotary, q_out=None, k_out=None, inverse=False, stre
 
     positions int32 [axes, B, N] or [axes, N] (the axis may be left out when there is one); rotary: a
     Rotary.  inverse turns back (the gradient).  q_out, k_out may be q, k
-    themselves.  Returns (q_out, k_out)."""
+    themselves.  Without tokens (B or N is 0) nothing is launched.  Returns
+    (q_out, k_out)."""
     dev = _device_of("q", q)
     B, Hq, N, d = q.shape
     if d != rotary.d:
@@ -494,6 +495,8 @@ def fa_rope(q, k, positions, rotary, q_out=None, k_out=None, inverse=False, stre
     elif k_out is not None:
         raise ValueError("k_out without k")
     pos, axis_stride, batch_stride = _rope_positions(positions, dev, rotary.axes, (B, N))
+    if B == 0 or N == 0:
+        return q_out, k_out
     _call(dev, stream, (_lib or load_library()).fa_rope, qp, qs, qop, qos, Hq, kp, ks, kop, kos, Hk, pos, axis_stride,
           batch_stride, B, N, d, rotary.rot, rotary.axes, rotary._freq, rotary._axis, rotary.interleaved, bool(inverse))
     return q_out, k_out
@@ -649,7 +652,8 @@ def fa_paged_append(q, k, v, k_cache, v_cache, slots, positions=None, rotary=Non
     is 1: views of one projection's output); caches [num_blocks, Hkv, block_size,
     d], bf16 or E4M3 codes (uint8) with k_descale, v_descale fp32 [Hkv];
     slots int32 [T], negative: the token is skipped and its q_out row left as
-    it was; positions int32 [axes, T] or [T].  Returns q_out (None without q)."""
+    it was; positions int32 [axes, T] or [T].  Without tokens (T = 0) nothing is
+    launched.  Returns q_out (None without q)."""
     dev = _device_of("k", k)
     T, Hkv, d = k.shape
     kp, ks = _strided("k", k, dev)
@@ -672,8 +676,11 @@ def fa_paged_append(q, k, v, k_cache, v_cache, slots, positions=None, rotary=Non
             raise ValueError("rotary needs positions, and the head dimension it was made for")
         rot, axes, freq, axis, interleaved = rotary.rot, rotary.axes, rotary._freq, rotary._axis, rotary.interleaved
         pos, axis_stride, _ = _rope_positions(positions, dev, axes, (T,))
+    slots_p = _flat("slots", slots, _I32, dev, T)
+    if T == 0:
+        return q_out
     _call(dev, stream, (_lib or load_library()).fa_paged_append, qp, qs, qop, qos, Hq, kp, ks, vp, vs, Hkv, kcp, vcp,
-          kind, kdp, vdp, _flat("slots", slots, _I32, dev, T), pos, axis_stride, T, num_blocks, block_size, d, rot,
+          kind, kdp, vdp, slots_p, pos, axis_stride, T, num_blocks, block_size, d, rot,
           axes, freq, axis, interleaved)
     return q_out
 
@@ -693,7 +700,8 @@ def fa_decode_paged(q, k_cache, v_cache, block_table, seq_lens, o=None, lse=None
     Hkv, block_size, d] with Hkv dividing Hq, bf16 or E4M3 codes (uint8) with
     k_descale, v_descale fp32 [Hkv]; block_table int32 [B, max_blocks],
     seq_lens int32 [B].  `workspace`: a contiguous CUDA uint8 tensor of
-    decode_paged_workspace bytes (allocated here if None).  Returns (o, lse)."""
+    decode_paged_workspace bytes (allocated here if None).  Without sequences
+    (B = 0) nothing is launched.  Returns (o, lse)."""
     dev = _device_of("q", q)
     B, Hq, Nq, d = q.shape
     qp, qs = _strided("q", q, dev)
@@ -705,6 +713,8 @@ def fa_decode_paged(q, k_cache, v_cache, block_table, seq_lens, o=None, lse=None
         o = _new((B, Hq, Nq, d), _BF16, dev, stream)
     if lse is None:
         lse = _new((B, Hq, Nq), _F32, dev, stream)
+    if B == 0:
+        return o, lse
     if workspace is None:
         workspace = _new(decode_paged_workspace(B, Hq, Hkv, Nq, d), _U8, dev, stream)
     op, os_ = _strided("o", o, dev, q.shape)
