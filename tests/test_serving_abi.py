@@ -208,6 +208,38 @@ def test_binding_refuses_host_tensors_and_other_types():
         ops.fa_block_tables(pos[None], pos, pos, pos, 16, 1)
 
 
+def test_a_call_makes_its_tensors_device_current(monkeypatch):
+    """Two devices, of which the second one holds the tensors: the C call and its stream are that one's."""
+    state = {"dev": 0}
+
+    class Device:
+        def __init__(self, dev):
+            self.dev = dev
+
+        def __enter__(self):
+            self.before, state["dev"] = state["dev"], self.dev
+
+        def __exit__(self, *exc):
+            state["dev"] = self.before
+
+    monkeypatch.setattr(ops, "_current_device", lambda: state["dev"])
+    monkeypatch.setattr(ops, "_raw_stream", lambda dev: 1000 + dev)
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    calls = []
+
+    def fn(*args):
+        calls.append((state["dev"], args))
+        return ops.FA_OK if args[0] != "bad" else INV
+
+    ops._call(1, None, fn, "x", 2)
+    ops._call(0, None, fn, "y")
+    ops._call(1, 77, fn, "z")
+    assert calls == [(1, ("x", 2, 1001)), (0, ("y", 1000)), (1, ("z", 77))] and state["dev"] == 0
+    with pytest.raises(ops.FAError):
+        ops._call(1, None, fn, "bad")
+    assert state["dev"] == 0
+
+
 def test_no_gpu_means_cuda_error(lib):
     if torch.cuda.is_available():
         pytest.skip("a GPU is present")
