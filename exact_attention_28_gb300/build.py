@@ -8,10 +8,10 @@ import subprocess
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB_PATH = os.path.join(HERE, "libfa_gb300.so")
-SOURCES = ["fa_api.cu", "fa_serving_api.cu"]
+SOURCES = ["fa_api.cu", "fa_serving_api.cu", "fa_decode_partly.cu"]
 DEPENDS = [*SOURCES, "fa_fwd_kernel.cuh", "fa_bwd_kernel.cuh", "fa_fp8_quant.cuh", "fa_rope_kernel.cuh",
-           "fa_block_tables_kernel.cuh", "fa_decode_kernel.cuh", "rotary_phase.h", "ptx_sm103.cuh",
-           os.path.join("..", "..", "include", "fa.h")]
+           "fa_block_tables_kernel.cuh", "fa_decode_kernel.cuh", "fa_decode_select.cuh", "rotary_phase.h",
+           "ptx_sm103.cuh", os.path.join("..", "..", "include", "fa.h")]
 
 
 def nvcc_command(out: str = LIB_PATH, extra=()):

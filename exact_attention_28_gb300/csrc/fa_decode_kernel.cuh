@@ -37,10 +37,12 @@
 // 64 sequences of 0 to 8192 keys, 32 query and 8 key heads, d = 128, bf16, 16-key
 // blocks: 159.7 us, 6.73 TB/s (the measured copy rate is 6.69); one of 131,035
 // keys 81.2 us (99%); 48 of 3 to 6007 keys, 16 heads, d = 64, E4M3, 4 new tokens
-// 51.8 us, 5.72 TB/s (86%).  64 sequences and 8 key heads with more query rows,
-// d = 128, of the copy rate: bf16 16 rows 95%, 24 92%, 32 88%, 40 68%, 64 56%;
-// E4M3 83%, 72%, 55%, 44%, 34%: from 32 rows on (E4M3: 24) mma.sync, at 8 cycles
-// of an SM's quarter each, is what bounds it, with the conversions beside it.
+// 51.9 us, 5.71 TB/s (85%).  The 64 sequences with 64 query and 8 key heads and
+// 2, 3, 4, 5 and 8 new tokens (16, 24, 32, 40 and 64 rows), d = 128, of the copy
+// rate: bf16 95%, 92%, 87%, 65%, 55%; E4M3 83%, 71%, 55%, 43%, 35%.  From 32 rows
+// on (E4M3: 24) mma.sync, at 8 cycles of an SM's quarter each, is what bounds it,
+// with the conversions beside it, which each of a team's warps repeats; and from
+// 33 rows on at d = 128 an SM holds two CTAs of two stages, 64 KB on the way.
 #pragma once
 
 #include <cstdint>
@@ -148,9 +150,10 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
     return r;
 }
-__device__ __forceinline__ float quad_max(float x) {
-    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-    return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+// 0xff.. at the elements of a word (two bf16, four E4M3 codes) that are NaN or infinite.
+template <bool F8>
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) {
+    return F8 ? __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu) : __vcmpeq2(w & 0x7f807f80u, 0x7f807f80u);
 }
 // Over the eight lanes of a warp that have the same lane % 4.
 __device__ __forceinline__ float column_max(float x) {
@@ -255,6 +258,35 @@ __device__ __forceinline__ float log_sum(float m, float sum) {
     return sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
 }
 
+// Adds the values that are not finite, of the newest keys that not every row
+// sees, to the rows that see them: to O, or (part >= 0) to the partial results
+// from row `part` on.  The whole CTA calls it, after rows [row0, row0 + n_rows)
+// of this item were written; a thread has its channels to itself.
+template <int D, bool F8>
+__device__ __noinline__ void add_not_finite(const DecodeParams &p, int b, int h, int len, int64_t part, int row0, int n_rows) {
+    const int first = len - p.Nq + 1;          // keys that row n sees end at first + n
+    for (int c = threadIdx.x; c < D; c += kDecodeThreads)
+        for (int r = 0; r < n_rows; ++r) {
+            const int head = (row0 + r) / p.Nq, n = row0 + r - head * p.Nq;
+            float x = 0.f;
+            for (int key = max(first, 0); key < first + n; ++key) {
+                const int page = p.block_table[static_cast<int64_t>(b) * p.max_blocks + (key >> p.block_shift)];
+                if (page < 0 || page >= p.num_blocks) continue;
+                const int64_t at = (((static_cast<int64_t>(page) * p.Hkv + h) << p.block_shift) +
+                                    (key & ((1 << p.block_shift) - 1))) * D + c;
+                const uint32_t v = F8 ? static_cast<const uint8_t *>(p.v_cache)[at] : static_cast<const uint16_t *>(p.v_cache)[at];
+                if (dec::not_finite<F8>(v) & 1) x += __uint_as_float(F8 ? 0x7fc00000u : v << 16);
+            }
+            if (x == 0.f) continue;
+            if (part >= 0) {
+                p.part_o[(part + r) * D + c] += x;
+            } else {
+                __nv_bfloat16 &o = p.o[b * p.os[0] + (h * p.group + head) * p.os[1] + n * p.os[2] + c];
+                o = __float2bfloat16_rn(__bfloat162float(o) + x);
+            }
+        }
+}
+
 // O = 0, LSE = -inf for every row of sequence b, which has no keys.
 template <int D>
 __device__ void write_empty_sequence(const DecodeParams &p, int b) {
@@ -268,7 +300,11 @@ __device__ void write_empty_sequence(const DecodeParams &p, int b) {
 
 // RW warps of a team share their quarters of a tile; each has 8 NT of the
 // 8 NT RW query rows.  RW = 1: four teams of one warp, each with its own keys.
-template <int D, int NT, int RW, bool F8>
+// PARTLY: the newest keys are masked for some rows (several causal new tokens).
+// One new token has no such keys, and pays nothing for them in a kernel of its
+// own: one short sequence 4.5 us (with PARTLY's code 4.6), 4000 of up to 20
+// keys 155 us (163).
+template <int D, int NT, int RW, bool F8, bool PARTLY>
 __global__ void __launch_bounds__(kDecodeThreads, (DecodeConfig<D, NT, RW, F8>::kCtasPerSm)) fa_decode_kernel(const __grid_constant__ DecodeParams p) {
     using C = DecodeConfig<D, NT, RW, F8>;
     constexpr int kTeams = kDecodeWarps / RW;
@@ -292,6 +328,7 @@ __global__ void __launch_bounds__(kDecodeThreads, (DecodeConfig<D, NT, RW, F8>::
     __shared__ int64_t sm_scan[kDecodeWarps];
     __shared__ int sm_first_b;
     __shared__ int64_t sm_first_u;
+    __shared__ int sm_taken_out;               // values that are not finite were, in this segment (PARTLY)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
     const int cta = blockIdx.x, ctas = gridDim.x;
 
@@ -509,6 +546,7 @@ __global__ void __launch_bounds__(kDecodeThreads, (DecodeConfig<D, NT, RW, F8>::
         if (segment_start < 0) {
             __syncthreads();     // every warp's part of the queries is there
             segment_start = cur.j;
+            if (PARTLY && tid == 0) sm_taken_out = 0;
             lim_all = p.causal ? cur.len - p.Nq + 1 : cur.len;
             if constexpr (F8) {
                 // q to fp16, scaled by a power of two so that the row's
@@ -574,6 +612,32 @@ __global__ void __launch_bounds__(kDecodeThreads, (DecodeConfig<D, NT, RW, F8>::
         else if constexpr (RW == 4) __syncthreads();
         else asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(RW * 32) : "memory");
         issue(stage == 0 ? C::kStages - 1 : stage - 1);      // the stage used up last
+
+        // The newest keys, which only the later of several new tokens see: a
+        // weight of 0 does not mask a value that is not finite.  Such values are
+        // taken out of the tile, and added to the rows that see them at the
+        // segment's end.  (The warps of a team do it side by side.)
+        if (PARTLY && (cur.j + 1) * C::kTile > lim_all) {
+            const int team0 = cur.j * C::kTile + team * RW * C::kKeys, lo = max(lim_all - team0, 0);
+            const int pieces = (min(cur.len - team0, RW * C::kKeys) - lo) * C::kChunks;
+            #pragma unroll 1
+            for (int x = lane; x < pieces; x += 32) {
+                const int k = lo + x / C::kChunks;
+                const uint32_t at = ring0 + stage * C::kStageBytes + (team * RW + k / C::kKeys) * C::kWarpBytes +
+                                    C::kWarpBytes / 2 + C::at(k % C::kKeys, x % C::kChunks);
+                uint32_t w[4], bad[4];
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                             : "r"(at) : "memory");
+                #pragma unroll
+                for (int i = 0; i < 4; ++i) bad[i] = dec::not_finite<F8>(w[i]);
+                if (bad[0] | bad[1] | bad[2] | bad[3]) {
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[0] & ~bad[0]), "r"(w[1] & ~bad[1]),
+                                 "r"(w[2] & ~bad[2]), "r"(w[3] & ~bad[3]) : "memory");
+                    sm_taken_out = 1;
+                }
+            }
+            __syncwarp();
+        }
 
         // Scores and outputs are held transposed, keys and channels down the
         // 16 rows of a product and 8 query rows across: a key's or value's
@@ -825,6 +889,7 @@ __global__ void __launch_bounds__(kDecodeThreads, (DecodeConfig<D, NT, RW, F8>::
             first_segment = false;
             segment_start = -1;
             __syncthreads();
+            if (PARTLY && sm_taken_out) add_not_finite<D, F8>(p, cur.b, cur.h, cur.len, whole ? -1 : part0, row0, n_rows);
         }
         advance<C::kTile>(p, cur);
     }

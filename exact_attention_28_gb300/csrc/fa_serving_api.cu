@@ -5,12 +5,13 @@
 #include <cstdint>
 #include <cstring>
 #include <mutex>
+#include <type_traits>
 
 #include <cuda_runtime.h>
 
 #include "../../include/fa.h"
 #include "fa_block_tables_kernel.cuh"
-#include "fa_decode_kernel.cuh"
+#include "fa_decode_select.cuh"
 #include "fa_rope_kernel.cuh"
 #include "rotary_phase.h"
 
@@ -42,6 +43,11 @@ cudaError_t launch_dependent(cudaStream_t stream, dim3 grid, int threads, int sm
 }
 
 template <class P>
+int rope_index(int d, bool interleaved) {
+    const int kind = std::is_same<P, fa::RopeParams>::value ? 0 : std::is_same<P, fa::AppendParams<false>>::value ? 1 : 2;
+    return 48 + 4 * kind + (d == 128 ? 2 : 0) + (interleaved ? 1 : 0);
+}
+template <class P>
 const void *rope_kernel(int d, bool interleaved) {
     return d == 128 ? (interleaved ? reinterpret_cast<const void *>(fa::fa_rope_kernel<128, true, P>)
                                    : reinterpret_cast<const void *>(fa::fa_rope_kernel<128, false, P>))
@@ -49,80 +55,38 @@ const void *rope_kernel(int d, bool interleaved) {
                                    : reinterpret_cast<const void *>(fa::fa_rope_kernel<64, false, P>));
 }
 
-// What the host needs to know of a decode kernel.
-struct DecodeKernel {
-    const void *fn;
-    int tile, ctas_per_sm, smem;
-};
-template <int D, int NT, int RW, bool F8>
-DecodeKernel decode_kernel_of() {
-    using C = fa::DecodeConfig<D, NT, RW, F8>;
-    return {reinterpret_cast<const void *>(fa::fa_decode_kernel<D, NT, RW, F8>), C::kTile, C::kCtasPerSm, C::kSmemBytes};
-}
+using fa::DecodeKernel;
+using fa::DecodeLayout;
+using fa::decode_layout;
+using fa::decode_rows;
 
-// How a key head's query rows lie on warps: `tiles` of 8 rows to a warp, and
-// `warps` warps that share a key range (and each load and convert all of it).
-// More tiles need fewer loads and more registers, at three only two CTAs an SM
-// at d = 128.  20 rows, d = 128, bf16 / E4M3: three tiles 170 / 110 us, two tiles
-// on two warps 180 / 160; 32 rows: two on two 191 / 158, four on one 248 / 228;
-// 40 rows: three on two 240 / 185, two on four 306 / 239.
-struct DecodeLayout {
-    int index, tiles, warps;
-};
-constexpr DecodeLayout kDecodeLayouts[6] = {{0, 1, 1}, {1, 2, 1}, {2, 3, 1}, {3, 2, 2}, {4, 3, 2}, {5, 2, 4}};
-int decode_rows(const DecodeLayout &l) { return 8 * l.tiles * l.warps; }
-// The first that holds the rows; more than the last one's go to further row
-// blocks, which read the keys again.
-DecodeLayout decode_layout(int rows) {
-    for (const DecodeLayout &l : kDecodeLayouts)
-        if (rows <= decode_rows(l)) return l;
-    return kDecodeLayouts[5];
-}
-template <int D, bool F8>
-DecodeKernel decode_kernel(const DecodeLayout &l) {
-    constexpr const DecodeLayout *k = kDecodeLayouts;
-    switch (l.index) {
-        case 0: return decode_kernel_of<D, k[0].tiles, k[0].warps, F8>();
-        case 1: return decode_kernel_of<D, k[1].tiles, k[1].warps, F8>();
-        case 2: return decode_kernel_of<D, k[2].tiles, k[2].warps, F8>();
-        case 3: return decode_kernel_of<D, k[3].tiles, k[3].warps, F8>();
-        case 4: return decode_kernel_of<D, k[4].tiles, k[4].warps, F8>();
-        default: return decode_kernel_of<D, k[5].tiles, k[5].warps, F8>();
-    }
-}
-
-// SM count of the current device, and the shared-memory limits of every
-// kernel that needs them set there (once per device).
+// SM count of a device, and which kernels have their shared-memory limits set
+// there: at a kernel's first call, for it loads the file that the kernel is in
+// (the 24 attention kernels of one file take 9 ms).
 struct ServingDevice {
     int sms = 0;
+    uint64_t ready = 0;
 };
 std::mutex g_serving_mu;
 ServingDevice g_serving[64];
 
-fa_status serving_device(int &sms) {
+// The current device's SM count, with `kernel` ready to run there.  `index`
+// numbers the kernels: 0 to 47 attention, 48 to 59 rotation.
+fa_status serving_device(int &sms, int index, const void *kernel, int smem) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return FA_ERR_CUDA;
     std::lock_guard<std::mutex> lock(g_serving_mu);
     ServingDevice &info = g_serving[dev];
-    if (info.sms == 0) {
-        int n = 0;
-        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return FA_ERR_CUDA;
-        for (const DecodeLayout &l : kDecodeLayouts)
-            for (const DecodeKernel &k : {decode_kernel<64, false>(l), decode_kernel<64, true>(l),
-                                          decode_kernel<128, false>(l), decode_kernel<128, true>(l)})
-                if (cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem) != cudaSuccess ||
-                    cudaFuncSetAttribute(k.fn, cudaFuncAttributePreferredSharedMemoryCarveout, 100) != cudaSuccess)
-                    return FA_ERR_CUDA;
-        for (int d : {64, 128})
-            for (bool interleaved : {false, true})
-                for (const void *k : {rope_kernel<fa::RopeParams>(d, interleaved),
-                                      rope_kernel<fa::AppendParams<false>>(d, interleaved),
-                                      rope_kernel<fa::AppendParams<true>>(d, interleaved)})
-                    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, fa::kRopeSmemBytes) !=
-                            cudaSuccess ||
-                        cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, 100) != cudaSuccess)
-                        return FA_ERR_CUDA;
-        info.sms = n;
+    if (info.sms == 0 &&
+        cudaDeviceGetAttribute(&info.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        info.sms = 0;
+        return FA_ERR_CUDA;
+    }
+    if (!(info.ready >> index & 1)) {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+            cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100) != cudaSuccess)
+            return FA_ERR_CUDA;
+        info.ready |= uint64_t{1} << index;
     }
     sms = info.sms;
     return FA_OK;
@@ -208,8 +172,9 @@ int64_t whole_bytes(const int64_t *strides, const int *extent, int n, int d) {
 // 768 (2) 7.9.
 template <class P>
 fa_status launch_rope(P &p, int d, bool interleaved, cudaStream_t stream) {
+    const void *const kernel = rope_kernel<P>(d, interleaved);
     int sms;
-    const fa_status st = serving_device(sms);
+    const fa_status st = serving_device(sms, rope_index<P>(d, interleaved), kernel, fa::kRopeSmemBytes);
     if (st != FA_OK) return st;
     const int64_t tiles = (static_cast<int64_t>(p.tokens) + fa::rope_tokens(d) - 1) / fa::rope_tokens(d);
     const auto groups = [&](int n) { return (static_cast<int64_t>(p.heads) + n - 1) / n; };
@@ -219,7 +184,7 @@ fa_status launch_rope(P &p, int d, bool interleaved, cudaStream_t stream) {
     const int64_t ctas = tiles * groups(p.per_cta);
     if (ctas > 0x7fffffff) return FA_ERR_INVALID_ARG;
     if (launch_dependent(stream, dim3(static_cast<unsigned>(ctas)), fa::kRopeThreads, fa::kRopeSmemBytes,
-                         rope_kernel<P>(d, interleaved), &p) != cudaSuccess)
+                         kernel, &p) != cudaSuccess)
         return FA_ERR_CUDA;
     return launched();
 }
@@ -517,8 +482,8 @@ extern "C" fa_status fa_decode_paged(const void *Q, const int64_t *q_strides, co
     p.row_blocks = (p.rows + cap - 1) / cap;
     p.part_rows = p.rows < cap ? p.rows : cap;
     // at most so many units as the table is wide: a CTA each, up to as many as fit the GPU
-    const DecodeKernel kernel = f8 ? (d == 64 ? decode_kernel<64, true>(layout) : decode_kernel<128, true>(layout))
-                                   : (d == 64 ? decode_kernel<64, false>(layout) : decode_kernel<128, false>(layout));
+    const bool partly = causal != 0 && Nq > 1;
+    const DecodeKernel kernel = partly ? fa::decode_kernel_partly(d, f8, layout) : fa::decode_kernel<false>(d, f8, layout);
     const int64_t tiles = (static_cast<int64_t>(max_blocks) * block_size + kernel.tile - 1) / kernel.tile;
     p.whole_items = tiles <= kDecodeWholeTiles;
     const int64_t units = (p.whole_items ? 1 : tiles + fa::kDecodeItemUnits) * p.row_blocks * Hkv * B;
@@ -531,7 +496,7 @@ extern "C" fa_status fa_decode_paged(const void *Q, const int64_t *q_strides, co
     if (p.c2 < 1.1754943508222875e-38f) p.c2 = 1.1754943508222875e-38f;
     p.q_sign = scale < 0.f ? 0x80008000u : 0u;
     int sms;
-    st = serving_device(sms);
+    st = serving_device(sms, 8 * layout.index + 4 * partly + 2 * f8 + (d == 128), kernel.fn, kernel.smem);
     if (st != FA_OK) return st;
     p.q = static_cast<const __nv_bfloat16 *>(Q);
     p.o = static_cast<__nv_bfloat16 *>(O);

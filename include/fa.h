@@ -522,8 +522,9 @@ fa_status fa_paged_append(const void *Q, const int64_t *q_strides, void *Qr, con
  * be Q itself with the same strides.
  * Cache rows at and past a sequence's length are not read: they may hold
  * anything.  A NaN among a row's query and the keys that it sees makes its O
- * and LSE NaN, so that LSE = -inf keeps its meaning.  The result does not
- * depend on what else is in the batch beyond the order in which slices are
+ * and LSE NaN, so that LSE = -inf keeps its meaning; keys that it does not see
+ * leave it as it is, be they and their values finite or not.  The result does
+ * not depend on what else is in the batch beyond the order in which slices are
  * joined; the same call gives the same bits.
  * Errors: as fa_fwd_paged; FA_ERR_UNSUPPORTED also for Nq > 16;
  * FA_ERR_INVALID_ARG for Hq % Hkv, cache_type, a NULL descale with
