@@ -15,7 +15,8 @@
 //   cache whatever the type; the C CTAs take equal runs of the list of all
 //   units, so a long sequence spreads over the GPU and short ones share a CTA.
 // * A CTA has two tiles of 32 KB, one in use and one on its way by 16-byte
-//   asynchronous copies, and three CTAs share an SM: 96 KB in flight on each.
+//   asynchronous copies, and three CTAs share an SM: 96 KB in flight on each
+//   (DecodeConfig: where three do not fit, two, with a third tile if that fits).
 //   (16 KB tiles cost 15 to 35% on 48 x 16 heads of up to 6007 keys in E4M3.)
 //   Each warp copies and (with up to 24 rows) uses its own quarter of a tile,
 //   so warps wait for nobody inside a segment.  An item's queries come the
@@ -23,9 +24,8 @@
 //   an item under the cache's traffic.
 //   Copies of keys past the end or of unallocated blocks are zero-filled
 //   instead: nothing behind a sequence's end is read.
-// * The products run on mma.sync: the 4 to 48 rows that a group of query heads
-//   has are a small part of the tcgen05 tile, and up to about 24 rows the tensor
-//   pipe is not what limits.  Scores and outputs are held transposed, with keys
+// * The products run on mma.sync: up to 32 rows of a key head (E4M3: 16) the
+//   tensor pipe is not what limits.  Scores and outputs are held transposed, with keys
 //   (channels of O) down the 16 rows of a product and 8 query rows across: a
 //   fragment of the cache, once loaded and converted, serves all of a warp's
 //   rows, and their number is rounded up to 8 only.  (16 query rows down: 82.3
@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(kDecodeThreads, (DecodeConfig<D, NT, RW, F8>::
     // ---- this CTA's run [u0, u1) of the units, and the sequence of the first
     const int64_t heads = static_cast<int64_t>(p.Hkv) * p.row_blocks;
     static_assert(kDecodeLeastUnits == 2, "a shift below");
-    int active, first_b = 0;                   // CTAs with units, kDecodeLeastUnits or more each
+    int active, first_b = 0;                   // CTAs with units: kDecodeLeastUnits or more each, one of them less if the total is odd
     int64_t units = 0, u0, u1, first_u = 0;    // first_u: where u0 lies among the units of sequence first_b
     const auto take_run = [&] {
         active = static_cast<int>(min(static_cast<int64_t>(ctas), p.whole_items ? units : (units + 1) >> 1));
