@@ -523,9 +523,11 @@ fa_status fa_paged_append(const void *Q, const int64_t *q_strides, void *Qr, con
  * Cache rows at and past a sequence's length are not read: they may hold
  * anything.  A NaN among a row's query and the keys that it sees makes its O
  * and LSE NaN, so that LSE = -inf keeps its meaning; keys that it does not see
- * leave it as it is, be they and their values finite or not.  The result does
- * not depend on what else is in the batch beyond the order in which slices are
- * joined; the same call gives the same bits.
+ * leave it as it is, be they and their values finite or not.  Sums are fp32.
+ * Weights meet the values as two bf16 terms (bf16 cache) or in fp16, where those
+ * below 2^-31 of a row's largest count in LSE alone (E4M3 cache).
+ * The result does not depend on what else is in the batch beyond the order in
+ * which slices are joined; the same call gives the same bits.
  * Errors: as fa_fwd_paged; FA_ERR_UNSUPPORTED also for Nq > 16;
  * FA_ERR_INVALID_ARG for Hq % Hkv, cache_type, a NULL descale with
  * FA_CACHE_E4M3, |scale| log2(e) past fp32's range, a bad stride, a NULL or too

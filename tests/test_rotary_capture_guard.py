@@ -130,3 +130,26 @@ def test_trails_go_with_their_graphs(streams):
     assert count() == before
     rotated(torch.zeros(1, 2, 6, 64))                   # nothing to differentiate
     assert count() == before
+
+
+def test_trails_from_several_threads(streams):
+    import threading
+    leaf, wrong = leaf_of(), []
+
+    def work():
+        try:
+            for _ in range(300):
+                grad(rotated(leaf[:, :2]), leaf)
+        except Exception as e:      # noqa: BLE001
+            wrong.append(e)
+
+    threads = [threading.Thread(target=work) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for i in range(300):            # another stream's rotations, and captures, at the same time
+        streams.on(i % 3)
+        y = rotated(leaf_of())
+        ops._meets(ops._leave_trail(y.grad_fn.next_functions, -1))
+    for t in threads:
+        t.join()
+    assert not wrong
