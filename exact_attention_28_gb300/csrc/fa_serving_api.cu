@@ -92,8 +92,8 @@ fa_status serving_device(int &sms, int index, const void *kernel, int smem) {
     return FA_OK;
 }
 
-// Memory that a call reads or writes; at nullptr, or with no bytes: none, or
-// not told apart here (a strided tensor's rows may lie between other ones').
+// Memory that a call reads or writes, none at nullptr or without bytes.  Of a
+// strided tensor only the first row: its others may lie between another's.
 struct Span {
     const void *at;
     int64_t bytes;
@@ -155,11 +155,11 @@ bool in_place_ok(const void *&in, const int64_t *in_strides, const void *out, co
     return true;
 }
 
-// Bytes of a bf16 tensor [extent_0, .., extent_{n-1}, d] where it is contiguous, else 0.
-int64_t whole_bytes(const int64_t *strides, const int *extent, int n, int d) {
+// Bytes of a bf16 tensor [extent_0, .., extent_{n-1}, d], of its first row unless it is contiguous.
+int64_t span_bytes(const int64_t *strides, const int *extent, int n, int d) {
     int64_t s = d;
     for (int i = n - 1; i >= 0; --i) {
-        if (extent[i] > 1 && strides[i] != s) return 0;
+        if (extent[i] > 1 && strides[i] != s) return 2 * d;
         s *= extent[i];
     }
     return 2 * s;
@@ -303,8 +303,8 @@ extern "C" fa_status fa_rope(const void *Q, const int64_t *q_strides, void *Qr, 
         return FA_ERR_MISALIGNED;
     const void *q_in = Q, *k_in = K;
     if (!in_place_ok(q_in, p.qs, Qr, p.qos, qe, 3) || !in_place_ok(k_in, p.ks, Kr, p.kos, ke, 3) || Qr == Kr ||
-        !apart<4>({{q_in, whole_bytes(p.qs, qe, 3, d), false}, {k_in, whole_bytes(p.ks, ke, 3, d), false},
-                   {Qr, whole_bytes(p.qos, qe, 3, d), true}, {Kr, whole_bytes(p.kos, ke, 3, d), true}}))
+        !apart<4>({{q_in, span_bytes(p.qs, qe, 3, d), false}, {k_in, span_bytes(p.ks, ke, 3, d), false},
+                   {Qr, span_bytes(p.qos, qe, 3, d), true}, {Kr, span_bytes(p.kos, ke, 3, d), true}}))
         return FA_ERR_INVALID_ARG;
     p.q = static_cast<const __nv_bfloat16 *>(Q);
     p.k = static_cast<const __nv_bfloat16 *>(K);
@@ -362,9 +362,9 @@ extern "C" fa_status fa_paged_append(const void *Q, const int64_t *q_strides, vo
     const void *q_in = Q;
     const int64_t cache = rows * Hkv * d * (cache_type == FA_CACHE_E4M3 ? 1 : 2);
     if (!in_place_ok(q_in, strides[0], Qr, strides[1], qe, 2) ||
-        !apart<7>({{q_in, whole_bytes(strides[0], qe, 2, d), false}, {K, whole_bytes(strides[2], ke, 2, d), false},
-                   {V, whole_bytes(strides[3], ke, 2, d), false}, {slots, int64_t{4} * T, false},
-                   {Qr, whole_bytes(strides[1], qe, 2, d), true}, {K_cache, cache, true}, {V_cache, cache, true}}))
+        !apart<7>({{q_in, span_bytes(strides[0], qe, 2, d), false}, {K, span_bytes(strides[2], ke, 2, d), false},
+                   {V, span_bytes(strides[3], ke, 2, d), false}, {slots, int64_t{4} * T, false},
+                   {Qr, span_bytes(strides[1], qe, 2, d), true}, {K_cache, cache, true}, {V_cache, cache, true}}))
         return FA_ERR_INVALID_ARG;
     const auto run = [&](auto p) {
         p.q = static_cast<const __nv_bfloat16 *>(Q);
@@ -472,9 +472,9 @@ extern "C" fa_status fa_decode_paged(const void *Q, const int64_t *q_strides, co
     // O may be Q: only an item's own CTAs read its queries, and its O is written when they are done
     const void *q_in = Q;
     if (!in_place_ok(q_in, p.qs, O, p.os, e, 3) ||
-        !apart<8>({{q_in, whole_bytes(p.qs, e, 3, d), false}, {K_cache, cache, false}, {V_cache, cache, false},
+        !apart<8>({{q_in, span_bytes(p.qs, e, 3, d), false}, {K_cache, cache, false}, {V_cache, cache, false},
                    {block_table, int64_t{4} * B * max_blocks, false}, {seq_lens, int64_t{4} * B, false},
-                   {O, whole_bytes(p.os, e, 3, d), true}, {LSE, int64_t{4} * B * Hq * Nq, true},
+                   {O, span_bytes(p.os, e, 3, d), true}, {LSE, int64_t{4} * B * Hq * Nq, true},
                    {workspace, static_cast<int64_t>(space.bytes), true}}))
         return FA_ERR_INVALID_ARG;
     const DecodeLayout layout = decode_layout(p.rows);

@@ -699,9 +699,9 @@ def fa_decode_paged(q, k_cache, v_cache, block_table, seq_lens, o=None, lse=None
     q bf16 [B, Hq, Nq, d], any strides whose last is 1; caches [num_blocks,
     Hkv, block_size, d] with Hkv dividing Hq, bf16 or E4M3 codes (uint8) with
     k_descale, v_descale fp32 [Hkv]; block_table int32 [B, max_blocks],
-    seq_lens int32 [B].  `workspace`: a contiguous CUDA uint8 tensor of
-    decode_paged_workspace bytes (allocated here if None).  Without sequences
-    (B = 0) nothing is launched.  Returns (o, lse)."""
+    seq_lens int32 [B].  o may be q itself.  `workspace`: a contiguous CUDA
+    uint8 tensor of decode_paged_workspace bytes (allocated here if None).
+    Without sequences (B = 0) nothing is launched.  Returns (o, lse)."""
     dev = _device_of("q", q)
     B, Hq, Nq, d = q.shape
     qp, qs = _strided("q", q, dev)

@@ -384,9 +384,9 @@ fa_status fa_schedule(int B, int H, int Nq, int Nk, int d, int causal, int num_s
  * 16-byte boundaries); rows of an output do not lie on one another: of its
  * dimensions with an extent above 1, each stride is at least d plus what the
  * dimensions of smaller strides reach, sum (extent - 1) * stride.
- * FA_ERR_INVALID_ARG also for an output on another argument's memory, wherever
- * both are contiguous or begin at the same place (but for the in-place forms
- * that are allowed); between strided tensors that is the caller's to see to.
+ * FA_ERR_INVALID_ARG also for an output on another argument's memory (but for
+ * the in-place forms that are allowed), as far as contiguous tensors and the
+ * first rows of strided ones show it; the rest is the caller's to see to.
  */
 
 /* Element type of a paged cache. */

@@ -147,7 +147,9 @@ def no_gpu():
         (dict(qo=0x40000), True),                                       # q's output is k's
         (dict(qo=0x10000), False), (dict(qo=0x10000, qos=strides(0, 64, 256)), True),         # in place, strides differ
         (dict(qo=0x10080), True), (dict(qo=0x30000), True), (dict(ko=0x10000), True), (dict(qo=0x3f800), True),
-        (dict(ko=0x30000), False), (dict(qo=0x30000, qos=strides(0, 1024, 64)), False),       # strided: not told apart
+        (dict(ko=0x30000), False), (dict(qo=0x30000, qos=strides(0, 1024, 64)), True),
+        (dict(ko=0x10000, qs=strides(0, 64, 256), kos=strides(0, 64, 512)), True),            # strided, first rows alike
+        (dict(ko=0x10080, qs=strides(0, 1024, 128), kos=strides(0, 1024, 128)), False),       # rows between rows
     ]] + [("fa_paged_append", APPEND, APPEND_ARGS, kw, refused) for kw, refused in [
         (dict(qos=strides(64, 64)), True), (dict(qos=strides(256, 64)), False), (dict(qos=strides(64, 512)), False),
         (dict(qos=strides(64, 448)), True), (dict(vc=0x50000), True), (dict(vc=0x51000), True), (dict(vc=0x52000), False),
