@@ -442,10 +442,10 @@ def fa_block_tables(block_table, ctx_lens, new_lens, free_blocks, block_size, nu
         counts = _new(2, _I32, dev, stream)
     _call(dev, stream, (_lib or load_library()).fa_block_tables, _whole("block_table", block_table, _I32, dev),
           _flat("ctx_lens", ctx_lens, _I32, dev, B), _flat("new_lens", new_lens, _I32, dev, B),
-          None if free_blocks is None else _flat("free_blocks", free_blocks, _I32, dev, num_free), _flat("seq_lens", seq_lens, _I32, dev, B),
-          _flat("query_start", query_start, _I32, dev, B + 1), _flat("slots", slots, _I32, dev, num_tokens),
-          _flat("positions", positions, _I32, dev, num_tokens), _flat("counts", counts, _I32, dev, 2),
-          B, max_blocks, block_size, num_free, num_tokens)
+          None if free_blocks is None else _flat("free_blocks", free_blocks, _I32, dev, num_free),
+          _flat("seq_lens", seq_lens, _I32, dev, B), _flat("query_start", query_start, _I32, dev, B + 1),
+          _flat("slots", slots, _I32, dev, num_tokens), _flat("positions", positions, _I32, dev, num_tokens),
+          _flat("counts", counts, _I32, dev, 2), B, max_blocks, block_size, num_free, num_tokens)
     return seq_lens, query_start, slots, positions, counts
 
 
@@ -713,16 +713,17 @@ def fa_decode_paged(q, k_cache, v_cache, block_table, seq_lens, o=None, lse=None
         o = _new((B, Hq, Nq, d), _BF16, dev, stream)
     if lse is None:
         lse = _new((B, Hq, Nq), _F32, dev, stream)
+    op, os_ = _strided("o", o, dev, q.shape)
+    lens, lsep = _flat("seq_lens", seq_lens, _I32, dev, B), _flat("lse", lse, _F32, dev, B * Hq * Nq)
     if B == 0:
         return o, lse
     if workspace is None:
         workspace = _new(decode_paged_workspace(B, Hq, Hkv, Nq, d), _U8, dev, stream)
-    op, os_ = _strided("o", o, dev, q.shape)
     nbytes = workspace.numel()
     _call(dev, stream, (_lib or load_library()).fa_decode_paged, qp, qs, kcp, vcp, kind, kdp, vdp, table,
-          _flat("seq_lens", seq_lens, _I32, dev, B), op, os_, _flat("lse", lse, _F32, dev, B * Hq * Nq), B, Hq,
-          Hkv, Nq, block_table.shape[1], num_blocks, block_size, d, 1.0 / math.sqrt(d) if scale is None else scale,
-          bool(causal), _flat("workspace", workspace, _U8, dev, nbytes), nbytes)
+          lens, op, os_, lsep, B, Hq, Hkv, Nq, block_table.shape[1], num_blocks, block_size, d,
+          1.0 / math.sqrt(d) if scale is None else scale, bool(causal),
+          _flat("workspace", workspace, _U8, dev, nbytes), nbytes)
     return o, lse
 
 
